@@ -1159,7 +1159,7 @@ attn_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ KPara
                 const float L = ctl->red[wg][0][gtid] + ctl->red[wg][1][gtid] + ctl->red[wg][2][gtid] +
                                 ctl->red[wg][3][gtid];
                 const float mr = ctl->m_run[c];
-                const bool live = L > 0.f;
+                const bool live = L != 0.f;  // (a NaN sum is no empty row)
                 ctl->corr[c] = live ? p.out_scale / L : 0.f;
                 if (c < u.rows_valid)
                     lbase[out_row0 + c] = live ? (mr - kAdd0 + log2f(L)) * 0.69314718055994531f : -INFINITY;

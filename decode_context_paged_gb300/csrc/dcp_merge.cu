@@ -9,6 +9,7 @@
 #include <cmath>
 
 #include "dcp_internal.h"
+#include "dcp_merge_row.cuh"
 #include "dcp_ptx.cuh"
 
 namespace dcp {
@@ -42,9 +43,9 @@ lse_merge_kernel(int n_parts, int64_t rows, int slices, const float *__restrict_
     const int64_t col4 = (int64_t)sl * 32 * VEC + lane;  // lane's first float4; then + 32 k
 
     float mx = -INFINITY;
-    for (int d = lane; d < n_parts; d += 32) mx = fmaxf(mx, __ldg(lse_part + (int64_t)d * rows + row));
+    for (int d = lane; d < n_parts; d += 32) mx = max_or_nan(mx, __ldg(lse_part + (int64_t)d * rows + row));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    for (int o = 16; o > 0; o >>= 1) mx = max_or_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
 
     float4 *dst = reinterpret_cast<float4 *>(o_out) + row * vdim4 + col4;
     if (mx == -INFINITY) {

@@ -2,7 +2,8 @@
 //
 // Exact log-sum-exp recombination ("Serving Macaron-V1 at Scale", 5.2; "SGLang's path"):
 // M = max_i LSE_i, w_i = exp(LSE_i - M), LSE = M + ln sum w_i, O = sum w_i O_i / sum w_i,
-// summed in ascending i; parts with LSE = -inf weigh zero; all -inf gives O = 0, LSE = -inf.
+// summed in ascending i; parts with LSE = -inf weigh zero; all -inf gives O = 0, LSE = -inf.  A NaN
+// part makes the row NaN.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -11,6 +12,13 @@
 #include <cstdint>
 
 namespace dcp {
+
+// The larger of two numbers, NaN if either is: fmaxf would drop a NaN part beside empty ones.
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
 
 // Partial i's row starts at o + i * o_stride (floats) and its LSE at lse[i * lse_stride].
 // Lane owns float4 columns lane + 32k, k < 4.  `scale` multiplies the merged O.  kPar partial
@@ -23,9 +31,9 @@ __device__ __forceinline__ void warp_merge_row512(int n, const float *o, int64_t
                                                   __nv_bfloat16 *o_out16 = nullptr) {
     const int lane = threadIdx.x & 31;
     float mx = -INFINITY;
-    for (int i = lane; i < n; i += 32) mx = fmaxf(mx, __ldcg(lse + i * lse_stride));
+    for (int i = lane; i < n; i += 32) mx = max_or_nan(mx, __ldcg(lse + i * lse_stride));
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+    for (int s = 16; s > 0; s >>= 1) mx = max_or_nan(mx, __shfl_xor_sync(0xffffffffu, mx, s));
     auto put = [&](int i, float x, float y, float z, float w) {
         if (o_out16) {
             const __nv_bfloat162 a = __floats2bfloat162_rn(x, y), b = __floats2bfloat162_rn(z, w);

@@ -6,7 +6,7 @@
 //     s_ij = softmax_scale * (q_i[0:128] . k_nope_j,h + q_i[128:192] . k_rope_j)
 //     O_i = sum_j exp(s_ij - LSE_i) v_j,h,   LSE_i = ln sum_j exp(s_ij)
 // over the keys j <= n_k - n_q + i (causal: the queries are the request's last tokens) or all keys.
-// A row that sees no key gives O = 0, LSE = -inf.  k_rope is one row per token, shared by the heads,
+// A row that sees no key gives O = 0, LSE = -inf, one with a NaN or +inf score NaN.  k_rope is one row per token, shared by the heads,
 // and is read in place: no concatenated key is made.
 //
 // Design (GB300 / sm_103a).  Bound: the tensor cores (640 flops per key and query).  Measured: 8192
@@ -44,6 +44,7 @@
 #include <cstring>
 
 #include "dcp_internal.h"
+#include "dcp_merge_row.cuh"
 #include "dcp_ptx.cuh"
 #include "dcp_search.cuh"
 
@@ -722,7 +723,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                     const float2 ml = ctl->stat[t][row];
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ctl->stat_free[t]);
-                    const bool live = ml.y > 0.f;
+                    const bool live = ml.y != 0.f;  // (a NaN sum is no empty row)
                     const float inv = live ? 1.f / ml.y : 0.f;
                     const long long at = (q_row + kTile * t + row) * p.H + head;
                     const long long prow = (long long)split * p.n_q * p.H + at;
@@ -798,12 +799,12 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(int splits, long lon
     // rows of no request keep what they hold (and have no partials)
     if (row >= rows || row / H < (long long)__ldg(q_ptr) || row / H >= (long long)__ldg(q_ptr + B)) return;
     float mx = -INFINITY;
-    for (int i = lane; i < splits; i += 32) mx = fmaxf(mx, __ldg(part_lse + i * rows + row));
+    for (int i = lane; i < splits; i += 32) mx = max_or_nan(mx, __ldg(part_lse + i * rows + row));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    for (int o = 16; o > 0; o >>= 1) mx = max_or_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
-    if (mx > -INFINITY) {
+    if (mx != -INFINITY) {
         for (int i = 0; i < splits; ++i) {
             const float l = __ldg(part_lse + i * rows + row);
             if (l == -INFINITY) continue;
@@ -816,11 +817,11 @@ __global__ void __launch_bounds__(256) prefill_merge_kernel(int splits, long lon
             acc.w = fmaf(w, x.w, acc.w);
         }
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = mx != -INFINITY ? 1.f / sum : 0.f;  // (sum >= 1, or NaN)
     acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
     if (out_bf16) static_cast<uint2 *>(out)[row * (kV / 4) + lane] = make_uint2(bf16x2(acc.x, acc.y), bf16x2(acc.z, acc.w));
     else static_cast<float4 *>(out)[row * (kV / 4) + lane] = acc;
-    if (lane == 0) lse[row] = sum > 0.f ? mx + logf(sum) : -INFINITY;
+    if (lane == 0) lse[row] = mx != -INFINITY ? mx + logf(sum) : -INFINITY;
 }
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,

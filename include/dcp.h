@@ -261,7 +261,9 @@ size_t dcp_partial_decode_attn_workspace_size(int num_requests, int q_len, int n
  *     s_k = softmax_scale * kappa * (q . k_raw),  LSE_d = ln sum_k exp(s_k),
  *     O_d = sum_k exp(s_k - LSE_d) * kappa * v_raw[0:512]
  * with kappa = kv_scale for FP8-E4M3 pools and 1 for BF16.  A rank with no visible key
- * writes O_d = 0 and LSE_d = -inf.
+ * writes O_d = 0 and LSE_d = -inf; a row with a NaN or +inf score among its visible keys has
+ * O_d and LSE_d NaN, and the merges pass that on.  A key that a row masks causally weighs 0
+ * and its first 512 elements have to be finite.
  *   q        bf16 [num_requests][q_len][num_heads][576]
  *   seq_lens int32 [num_requests], tokens of b including the q_len new ones (>= q_len)
  *   req_page_ptr int64 [num_requests+1], dst_vpages int32 [num_pages]: page table
@@ -471,6 +473,7 @@ int dcp_decode_attn_merged_scaled(int num_requests, int q_len, int num_heads, co
  *     k_ptr[b] .. k_ptr[b+1] - 1; rows outside them are padding
  *   causal != 0: query i of a request sees keys j <= n_k(b) - n_q(b) + i (the queries are the last tokens
  *     of the keys' sequence); 0: all keys of the request.  A row that sees no key: out 0, lse -inf.
+ *     A row with a NaN or +inf score among the keys it sees: out and lse NaN.
  *   out [n_q][H][128] FP32, or BF16 rounded to nearest-even once (out_bf16), 16-byte aligned;
  *   lse fp32 [n_q][H].  Two such results over different keys combine exactly with dcp_lse_merge (v_dim 128).
  * Keys, and values of keys, that lie outside a row's request may hold anything.  A value a row masks
@@ -509,7 +512,7 @@ int dcp_reshard_scales(int num_requests, const int64_t *req_page_ptr, int64_t nu
  * recombination): per row r, M = max_d LSE_d, w_d = exp(LSE_d - M),
  *     LSE[r] = M + ln sum_d w_d,   O[r] = sum_d w_d O_d[r] / sum_d w_d,
  * summed in ascending d ([P1] 8: fixed rank order).  Parts with LSE = -inf weigh zero;
- * a row whose parts are all -inf gets O = 0, LSE = -inf.
+ * a row whose parts are all -inf gets O = 0, LSE = -inf; one with a NaN part is NaN.
  *   o_part fp32 [n_parts][rows][v_dim], lse_part fp32 [n_parts][rows]
  *   o_out  fp32 [rows][v_dim],           lse_out  fp32 [rows]
  *   1 <= n_parts <= 64, rows >= 0, v_dim in {128, 256, 512}; 16-byte aligned O arrays.

@@ -334,6 +334,7 @@ __device__ __forceinline__ void split_e4m3x4(float a, float b, float c, float d,
 
 // FP8 path: Q (BF16) -> hi and lo E4M3 rows scaled by a power of two per row so that the
 // row's largest magnitude lands in (224, 448]; q = (hi + lo) * 2^-qexp up to ~2^-8 relative.
+// NaN and infinite elements become NaN.
 // One warp per query row.  Output rows [0, R) = hi, [R, 2R) = lo; rscale[row] = 2^-qexp.
 __device__ void q_split_row(int row, int R, const __nv_bfloat16 *__restrict__ q, uint8_t *__restrict__ qhl,
                             float *__restrict__ rscale) {
@@ -357,17 +358,19 @@ __device__ void q_split_row(int row, int R, const __nv_bfloat16 *__restrict__ q,
         e = max(-100, min(100, e));
     }
     const float sc = ldexpf(1.f, e);
+    // (E4M3 has no infinity and would saturate: the row's scores are +-inf or NaN, its result NaN)
+    auto scaled = [&](float x) { return fabsf(x) == INFINITY ? NAN : x * sc; };
     uint8_t *hi = qhl + (long long)row * kKDim;
     uint8_t *lo = qhl + ((long long)R + row) * kKDim;
 #pragma unroll
     for (int k = 0; k < 9; ++k) {
         const int c = 2 * (lane + 32 * k);
-        const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * k] * sc, v[2 * k + 1] * sc),
-                                                                __NV_SATFINITE, __NV_E4M3);
+        const float a = scaled(v[2 * k]), b = scaled(v[2 * k + 1]);
+        const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
         const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3);
         const float2 hf = __half22float2(*reinterpret_cast<const __half2 *>(&hr));
         const __nv_fp8x2_storage_t l = __nv_cvt_float2_to_fp8x2(
-            make_float2(v[2 * k] * sc - hf.x, v[2 * k + 1] * sc - hf.y), __NV_SATFINITE, __NV_E4M3);
+            make_float2(a - hf.x, b - hf.y), __NV_SATFINITE, __NV_E4M3);
         *reinterpret_cast<__nv_fp8x2_storage_t *>(hi + c) = h;
         *reinterpret_cast<__nv_fp8x2_storage_t *>(lo + c) = l;
     }

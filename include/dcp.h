@@ -262,8 +262,9 @@ size_t dcp_partial_decode_attn_workspace_size(int num_requests, int q_len, int n
  *     O_d = sum_k exp(s_k - LSE_d) * kappa * v_raw[0:512]
  * with kappa = kv_scale for FP8-E4M3 pools and 1 for BF16.  A rank with no visible key
  * writes O_d = 0 and LSE_d = -inf; a row with a NaN or +inf score among its visible keys has
- * O_d and LSE_d NaN, and the merges pass that on.  A key that a row masks causally weighs 0
- * and its first 512 elements have to be finite.
+ * O_d and LSE_d NaN, and the merges pass that on (over E4M3 pools, whose codes have no infinity,
+ * an infinite query element counts as NaN).  A key that a row masks causally weighs 0, and its
+ * first 512 elements have to be finite.
  *   q        bf16 [num_requests][q_len][num_heads][576]
  *   seq_lens int32 [num_requests], tokens of b including the q_len new ones (>= q_len)
  *   req_page_ptr int64 [num_requests+1], dst_vpages int32 [num_pages]: page table

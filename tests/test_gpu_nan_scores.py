@@ -116,14 +116,15 @@ def test_decode_key(cuda_device, lens, T, H, N, layout, pos, form):
         assert all_nan(m[0], z[0]) and torch.equal(m[1], ref[0][1]) and torch.equal(z[1], ref[1][1])
 
 
+@pytest.mark.parametrize("value", [NAN, INF, -INF])
 @pytest.mark.parametrize("form", ["blocks", "one", "bf16"])
-def test_decode_query(cuda_device, form):
-    """A NaN in one query row stays in that row (an empty request's rows stay empty)."""
+def test_decode_query(cuda_device, form, value):
+    """A NaN or an infinity in one query row makes that row NaN, no other (an empty request's rows stay empty)."""
     c = Case([700, 0, 300], 2, 48, 3, 16, "page", cuda_device, seed=54)
     pools = c.pool if form != "bf16" else (c.pool.float() * 2.0 ** -7).to(torch.bfloat16)
     ref = decode(c, form, pools)
     for at in ((0, 1, 5), (1, 0, 0), (2, 0, 47)):
-        c.q[at][100] = NAN
+        c.q[at][100] = value
     o, lse, _, _ = decode(c, form, pools)
     rest = torch.ones(3, 2, 48, dtype=torch.bool, device=cuda_device)
     for at in ((0, 1, 5), (2, 0, 47)):

@@ -325,12 +325,12 @@ int dcp_reshard_scales(int num_requests, const int64_t *req_page_ptr, int64_t nu
         a.layer_start[r] = s;
         a.layer_start[r + 1] = e;
         a.src_scales[r] = src_scales[r];
-        if ((e > s) && (!src_scales[r] || !aligned(src_scales[r], 16))) return DCP_ERR_INVALID_ARG;
+        if ((e > s) && (!src_scales[r] || !aligned(src_scales[r], 4))) return DCP_ERR_INVALID_ARG;
     }
     a.src_pool_pages = src_pool_pages;
     a.n_dcp = n_dcp;
     for (int d = 0; d < n_dcp; ++d) {
-        if (!dst_scales[d] || !aligned(dst_scales[d], 16)) return DCP_ERR_INVALID_ARG;
+        if (!dst_scales[d] || !aligned(dst_scales[d], 4)) return DCP_ERR_INVALID_ARG;
         a.dst_scales[d] = dst_scales[d];
     }
     a.dst_slots = dst_slots_per_rank;

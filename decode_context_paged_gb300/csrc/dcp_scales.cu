@@ -6,7 +6,8 @@
 // [layers of r][source pages][64 / g], destination [layers][slots][64 / g] per rank.
 //
 // A gather and a scatter of 4 to 256 bytes per (layer, page).  One thread owns one vector (16 bytes,
-// or a whole page's scales where they are fewer) of one page and moves it for kLayersPerThread
+// or a whole page's scales where they are fewer, or what every rank's start is a multiple of: a rank's
+// scales may be a slice of a larger tensor) of one page and moves it for kLayersPerThread
 // layers: the page's two table entries and its division are paid once, and the loads of all those
 // layers are in flight together.  Bound: HBM for whole batches (neighbouring threads cover a
 // page's 256 contiguous bytes; 184 MB of scales in 58.5 us = 6.5 TB/s, 98% of the copy rate), latency
@@ -60,7 +61,11 @@ __global__ void __launch_bounds__(kScaleThreads) scales_kernel(const __grid_cons
 
 cudaError_t launch_scales(const ScalesArgs &a, cudaStream_t stream) {
     if (a.num_pages <= 0 || a.num_layers <= 0) return cudaSuccess;
-    const int vec = a.groups >= 4 ? 4 : a.groups;  // floats per thread
+    int vec = a.groups >= 4 ? 4 : a.groups;  // floats per thread
+    uintptr_t starts = 0;
+    for (int r = 0; a.layer_start[r] < a.num_layers; ++r) starts |= reinterpret_cast<uintptr_t>(a.src_scales[r]);
+    for (int d = 0; d < a.n_dcp; ++d) starts |= reinterpret_cast<uintptr_t>(a.dst_scales[d]);
+    while (starts % (4 * vec)) vec /= 2;  // (every start is a multiple of 4 bytes)
     const int vecs = a.groups / vec;
     const long long blocks = (a.num_pages * vecs + kScaleThreads - 1) / kScaleThreads;
     const int ly = (a.num_layers + kLayersPerThread - 1) / kLayersPerThread;

@@ -498,7 +498,8 @@ int dcp_prefill_attn(int num_requests, int64_t n_q, int64_t n_k, int num_heads, 
  * for their scales.
  *   src_scales (host array of n_cp device pointers): [layers of rank r][src_pool_pages][64 / scale_block]
  *   dst_scales (host array of n_dcp device pointers): [num_layers][dst_slots_per_rank][64 / scale_block]
- *   fp32, 16-byte aligned; layers are split over the CP ranks as dcp_layer_range does
+ *   fp32, 4-byte aligned (16 is fastest where a page has four scales or more); layers are split over
+ *   the CP ranks as dcp_layer_range does
  * Entries at or behind req_page_ptr[num_requests] are padding and are skipped; slots no entry names
  * are left as they were; an index outside its pool sets DCP_DEVERR_OUT_OF_RANGE and is skipped.
  * Returns DCP_ERR_INVALID_ARG, DCP_ERR_CUDA.

@@ -584,7 +584,7 @@ def partial_decode_attn(q: torch.Tensor, seq_lens: torch.Tensor, req_page_ptr: t
     _check_out(o_part, (N, B, T, H, V_DIM), "o_part")
     _check_out(lse_part, (N, B, T, H), "lse_part")
     dev = q.device
-    if planned and (layout == "token" or (kv_scales is not None and workspace is None)):
+    if planned and (layout == "token" or workspace is None):
         raise ValueError("a planned run needs the workspace holding the plan (page layout)")
     if kv_scales is not None:
         _device(q, "q")

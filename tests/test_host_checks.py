@@ -1,0 +1,30 @@
+"""CPU checks of the binding: calls that must be refused before anything is allocated or launched.  (The tensors are on the
+CPU: a check that comes too late shows as another error.)"""
+import pytest
+import torch
+
+import decode_context_paged_gb300 as dcp
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from decode_context_paged_gb300 import _build
+    _build.build()
+
+
+def attention(B=2, T=1, H=4, N=2, slots=3, dtype=torch.bfloat16):
+    return dict(q=torch.zeros(B, T, H, 576, dtype=torch.bfloat16), seq_lens=torch.ones(B, dtype=torch.int32),
+                req_page_ptr=torch.arange(B + 1), dst_vpages=torch.zeros(B, dtype=torch.int32),
+                kv_pools=[torch.zeros(slots, 64, 576, dtype=dtype) for _ in range(N)], softmax_scale=0.1)
+
+
+SCALED = dict(kv_scales=[torch.ones(3, 4) for _ in range(2)])
+
+
+@pytest.mark.parametrize("scaled", [False, True])
+@pytest.mark.parametrize("call", [dcp.partial_decode_attn, dcp.decode_attn_merged], ids=lambda f: f.__name__)
+def test_a_planned_run_needs_the_workspace_of_its_plan(call, scaled):
+    """Without it the call would run whatever plan a new allocation happens to hold."""
+    a = attention(dtype=torch.float8_e4m3fn if scaled else torch.bfloat16)
+    with pytest.raises(ValueError, match="planned run needs the workspace"):
+        call(**a, **(SCALED if scaled else {}), planned=True)

@@ -216,6 +216,14 @@ def _check_out(t: torch.Tensor | None, shape: tuple, name: str) -> None:
         raise ValueError(f"{name} must be float32 {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
 
 
+def _check_table(requests: int, seq_lens: torch.Tensor | None, req_page_ptr: torch.Tensor) -> None:
+    """The attention takes the number of requests from q and reads so many lengths and page offsets."""
+    if seq_lens is not None and seq_lens.numel() < requests:
+        raise ValueError(f"seq_lens holds {seq_lens.numel()} lengths of {requests} requests")
+    if requests > 0 and req_page_ptr.numel() <= requests:
+        raise ValueError(f"req_page_ptr holds {req_page_ptr.numel()} offsets, {requests} requests need {requests + 1}")
+
+
 def _pool_pages(t: torch.Tensor, name: str) -> tuple[int, int]:
     """(layers, pages) of a pool [layers][pages][64][576] (or [pages][64][576] as one layer)."""
     if t.dim() == 4 and tuple(t.shape[2:]) == (PAGE, K_DIM):
@@ -579,6 +587,7 @@ def partial_decode_attn(q: torch.Tensor, seq_lens: torch.Tensor, req_page_ptr: t
     B, T, H, kd = q.shape
     if kd != K_DIM:
         raise ValueError("q must be [B][T][H][576]")
+    _check_table(B, seq_lens, req_page_ptr)
     N = len(kv_pools)
     slots, dtype = _check_pools(kv_pools)
     _check_out(o_part, (N, B, T, H, V_DIM), "o_part")
@@ -631,6 +640,7 @@ def attn_plan(q_shape: tuple, req_page_ptr: torch.Tensor, dst_vpages: torch.Tens
     """The attention's plan for this page table into ``workspace`` (dcp_attn_plan); q_shape =
     (B, T, H); kv_pools give the DCP size, slots per rank and dtype."""
     B, T, H = q_shape[:3]
+    _check_table(B, None, req_page_ptr)
     _check_pools(kv_pools)
     _check(_load().dcp_attn_plan(B, T, H, _dptr(req_page_ptr, "req_page_ptr", torch.int64), dst_vpages.numel(),
                                  _dptr(dst_vpages, "dst_vpages", torch.int32), _kv_code(kv_pools[0]), len(kv_pools),
@@ -707,6 +717,7 @@ def decode_attn_merged(q: torch.Tensor, seq_lens: torch.Tensor, req_page_ptr: to
     B, T, H, kd = q.shape
     if kd != K_DIM:
         raise ValueError("q must be [B][T][H][576]")
+    _check_table(B, seq_lens, req_page_ptr)
     N = len(kv_pools)
     _check_out(o_part, (N, B, T, H, V_DIM), "o_part")
     _check_out(lse_part, (N, B, T, H), "lse_part")
@@ -760,6 +771,7 @@ def partial_decode_attn_static(q: torch.Tensor, seq_lens: torch.Tensor, req_page
     B, T, H, kd = q.shape
     if kd != K_DIM:
         raise ValueError("q must be [B][T][H][576]")
+    _check_table(B, seq_lens, req_page_ptr)
     N = len(kv_pools)
     slots, dtype = _check_pools(kv_pools)
     _check_out(o_part, (N, B, T, H, V_DIM), "o_part")

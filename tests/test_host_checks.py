@@ -28,3 +28,23 @@ def test_a_planned_run_needs_the_workspace_of_its_plan(call, scaled):
     a = attention(dtype=torch.float8_e4m3fn if scaled else torch.bfloat16)
     with pytest.raises(ValueError, match="planned run needs the workspace"):
         call(**a, **(SCALED if scaled else {}), planned=True)
+
+
+@pytest.mark.parametrize("short,what", [(dict(seq_lens=torch.ones(1, dtype=torch.int32)), "seq_lens holds 1"),
+                                        (dict(req_page_ptr=torch.arange(2)), "req_page_ptr holds 2")])
+@pytest.mark.parametrize("scaled", [False, True])
+@pytest.mark.parametrize("call", [dcp.partial_decode_attn, dcp.decode_attn_merged, dcp.partial_decode_attn_static],
+                         ids=lambda f: f.__name__)
+def test_lengths_and_offsets_of_every_request(call, scaled, short, what):
+    """The number of requests is q's: a shorter seq_lens or req_page_ptr would be read past its end."""
+    if scaled and call is dcp.partial_decode_attn_static:
+        pytest.skip("takes no block scales")
+    a = attention(dtype=torch.float8_e4m3fn if scaled else torch.bfloat16)
+    with pytest.raises(ValueError, match=what):
+        call(**{**a, **short}, **(SCALED if scaled else {}))
+
+
+def test_a_plan_needs_offsets_of_every_request():
+    a = attention()
+    with pytest.raises(ValueError, match="req_page_ptr holds 2"):
+        dcp.attn_plan((2, 1, 4), torch.arange(2), a["dst_vpages"], a["kv_pools"], torch.zeros(1 << 20, dtype=torch.uint8))

@@ -4,7 +4,8 @@
 // pointer from Python costs about half a microsecond a tensor: more than the call itself for a
 // decode step's small operators.  These functions answer for tensors that are as the call wants
 // them and return None otherwise; the binding then asks again in Python and raises the error, so
-// what is accepted is said in one place.  Outputs are allocated here too (1.3 us against torch.empty's
+// what is accepted is said in one place.  An exception that torch throws (a tensor without storage, as
+// inside torch.vmap) becomes the Python error that the same question gives there.  Outputs are allocated here too (1.3 us against torch.empty's
 // 1.7), and the serving calls go to the library without ctypes, which takes 1.5 to 3 us to convert 15
 // to 30 arguments: a call of append 16 -> 11.5 us, prompt attention 20 -> 11, decode 41 -> 30, scales
 // 6.5 -> 5.  The module is optional.
@@ -14,6 +15,7 @@
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/utils/object_ptr.h>
 
 #include <dlfcn.h>
 
@@ -42,36 +44,38 @@ bool read_type(PyObject *o, at::ScalarType *type) {
 
 // ptr(tensor, dtype, device) -> address of a contiguous tensor, or None
 PyObject *ptr(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
     at::ScalarType type;
     if (n != 3 || !is_tensor(args[0]) || !read_type(args[1], &type)) return none();
     const at::Tensor &t = THPVariable_Unpack(args[0]);
     if (!fits(t, type, PyLong_AsLong(args[2]))) return none();
     return PyLong_FromUnsignedLongLong(reinterpret_cast<uintptr_t>(t.data_ptr()));
+    END_HANDLE_TH_ERRORS
 }
 
 // ptrs(list, like, dtype, device) -> bytes of the addresses of contiguous tensors of like's shape, or None
 PyObject *ptrs(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
     at::ScalarType type;
     if (n != 4 || !PyList_Check(args[0]) || !is_tensor(args[1]) || !read_type(args[2], &type)) return none();
     const long dev = PyLong_AsLong(args[3]);
     const at::IntArrayRef shape = THPVariable_Unpack(args[1]).sizes();
     const Py_ssize_t count = PyList_GET_SIZE(args[0]);
-    PyObject *out = PyBytes_FromStringAndSize(nullptr, count * 8);
+    THPObjectPtr out(PyBytes_FromStringAndSize(nullptr, count * 8));
     if (!out) return nullptr;
-    uint64_t *p = reinterpret_cast<uint64_t *>(PyBytes_AS_STRING(out));
+    uint64_t *p = reinterpret_cast<uint64_t *>(PyBytes_AS_STRING(out.get()));
     for (Py_ssize_t i = 0; i < count; ++i) {
         PyObject *o = PyList_GET_ITEM(args[0], i);
-        if (!is_tensor(o) || !fits(THPVariable_Unpack(o), type, dev) || THPVariable_Unpack(o).sizes() != shape) {
-            Py_DECREF(out);
-            return none();
-        }
+        if (!is_tensor(o) || !fits(THPVariable_Unpack(o), type, dev) || THPVariable_Unpack(o).sizes() != shape) return none();
         p[i] = reinterpret_cast<uintptr_t>(THPVariable_Unpack(o).data_ptr());
     }
-    return out;
+    return out.release();
+    END_HANDLE_TH_ERRORS
 }
 
 // rows(tensor, width, dims, multiple, device) -> (address, outer strides...) of BF16 rows, or None
 PyObject *rows(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
     if (n != 5 || !is_tensor(args[0])) return none();
     const at::Tensor &t = THPVariable_Unpack(args[0]);
     const long width = PyLong_AsLong(args[1]), dims = PyLong_AsLong(args[2]), mult = PyLong_AsLong(args[3]);
@@ -84,6 +88,7 @@ PyObject *rows(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (s0 % mult || s1 % mult || p % (2 * mult)) return none();
     if (dims == 2) return Py_BuildValue("KL", (unsigned long long)p, (long long)s0);
     return Py_BuildValue("KLL", (unsigned long long)p, (long long)s0, (long long)s1);
+    END_HANDLE_TH_ERRORS
 }
 
 // empty(shape, dtype, device) -> a new contiguous tensor on that GPU, or None

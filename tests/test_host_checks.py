@@ -1,5 +1,9 @@
 """CPU checks of the binding: calls that must be refused before anything is allocated or launched.  (The tensors are on the
 CPU: a check that comes too late shows as another error.)"""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -48,3 +52,36 @@ def test_a_plan_needs_offsets_of_every_request():
     a = attention()
     with pytest.raises(ValueError, match="req_page_ptr holds 2"):
         dcp.attn_plan((2, 1, 4), torch.arange(2), a["dst_vpages"], a["kv_pools"], torch.zeros(1 << 20, dtype=torch.uint8))
+
+
+NO_STORAGE = """
+import sys
+import torch
+from torch._subclasses import FakeTensorMode
+import decode_context_paged_gb300 as dcp
+if dcp._views is None:
+    print("no helper")
+    sys.exit(0)
+with FakeTensorMode(allow_non_fake_inputs=True):
+    x = torch.empty(3, 4, 64, dtype=torch.bfloat16, device="cuda")
+questions = dict(ptr=lambda t: dcp._ptr(t, "t", torch.bfloat16, 0), ptrs=lambda t: dcp._ptrs([t], "t", t, torch.bfloat16, 0),
+                 rows=lambda t: dcp._rows(t, "t", 64, 2, 2, 0))
+def ask(t):
+    try:
+        questions[sys.argv[1]](t)
+    except RuntimeError as e:
+        print("raised", e)
+    return t
+torch.vmap(ask)(x)
+"""
+
+
+@pytest.mark.parametrize("question", ["ptr", "ptrs", "rows"])
+def test_a_tensor_without_storage_raises(question):
+    """Inside torch.vmap a tensor has no pointer: a Python error, not the end of the process."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", NO_STORAGE, question], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-500:]
+    if "no helper" in r.stdout:
+        pytest.skip("the C++ helper was not built here")
+    assert "raised" in r.stdout, r.stdout

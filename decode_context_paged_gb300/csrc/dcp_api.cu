@@ -41,6 +41,23 @@ void layer_range(int n_layers, int n_cp, int r, int *s, int *e) {
     *e = *s + base + (r < extra ? 1 : 0);
 }
 
+// Whether a row (t, h) of 64 elements, t < n, h < heads, at t * tok + h * head (strides >= 0) and another row
+// (t', h') that starts `apart` elements further can share memory; the same row, (t, h) = (t', h'), only if
+// it is shifted against itself.
+bool rows_meet(int64_t apart, int64_t n, int64_t tok, int64_t heads, int64_t head) {
+    if (apart == 0 && (heads == 1 || head >= 64) && (n == 1 || tok >= (heads - 1) * head + 64)) return false;  // token after token
+    for (int64_t dh = 1 - heads; dh < heads; ++dh) {
+        const int64_t x = apart + dh * head;  // a row dt tokens on starts x + dt * tok further
+        const int64_t near = n == 1 || tok == 0 ? 0 : -x / tok;
+        for (int64_t dt = near - 1; dt <= near + 1; ++dt) {
+            if (dt <= -n || dt >= n || (dh == 0 && dt == 0 && apart == 0)) continue;
+            const int64_t gap = x + dt * tok;
+            if (gap > -64 && gap < 64) return true;
+        }
+    }
+    return false;
+}
+
 // Tokens per block scale: a power of two up to the page.
 bool valid_scale_block(int g) { return g >= 1 && g <= kPage && (g & (g - 1)) == 0; }
 
@@ -357,9 +374,21 @@ int dcp_append_kv(int num_requests, int64_t num_new, const void *latent, int64_t
     if (latent_stride % 8 || rope_stride % 2) return DCP_ERR_INVALID_ARG;
     if (num_heads > 0 && (q_token_stride % 2 || q_head_stride % 2 || q_out_token_stride % 2 || q_out_head_stride % 2))
         return DCP_ERR_INVALID_ARG;
-    // rows that share memory would be written twice (a broadcast q_out)
+    // rows that share memory would be written twice (a broadcast q_out, strides that meet)
     if ((num_heads > 0 && num_new > 1 && q_out_token_stride < 64) || (num_heads > 1 && q_out_head_stride < 64))
         return DCP_ERR_INVALID_ARG;
+    if (num_heads > 0 && num_new > 0) {
+        // (an axis of one entry has no stride; no tensor is 2^40 elements wide, and the sums stay in range)
+        const int64_t tok = num_new > 1 ? q_out_token_stride : 0, head = num_heads > 1 ? q_out_head_stride : 0;
+        if (tok > (1LL << 40) / num_new || head > (1LL << 40) / num_heads) return DCP_ERR_INVALID_ARG;
+        if (rows_meet(0, num_new, tok, num_heads, head)) return DCP_ERR_INVALID_ARG;
+        // queries in place: row for row, or beside one another
+        const int64_t apart = (int64_t)(reinterpret_cast<uintptr_t>(q_out) - reinterpret_cast<uintptr_t>(q_rope)) / 2;
+        const int64_t span = (num_new - 1) * tok + (num_heads - 1) * head + 64;
+        const bool alike = (num_new == 1 || q_token_stride == tok) && (num_heads == 1 || q_head_stride == head);
+        if (alike ? apart > -span && apart < span && rows_meet(apart, num_new, tok, num_heads, head) : apart == 0 && q_out)
+            return DCP_ERR_INVALID_ARG;
+    }
     if (num_requests == 0 || num_new == 0) return DCP_OK;
     if (!latent || !rope || !new_ptr || !seq_lens || !req_page_ptr || !inv_freq || !kv_pools) return DCP_ERR_INVALID_ARG;
     if (num_pages > 0 && !dst_vpages) return DCP_ERR_INVALID_ARG;

@@ -424,7 +424,8 @@ int dcp_partial_decode_attn_static(int num_requests, int q_len, int num_heads, c
  *     the block's earlier rows are coded again as e4m3(code * old / new).
  *   num_heads > 0: q_rope [num_new][num_heads][64] BF16 (given strides, even; 4-byte aligned), the
  *     new tokens' queries, are rotated alike into q_out, which may be q_rope itself with the same
- *     strides; rows of q_out must not overlap (strides of at least 64).
+ *     strides; rows of q_out that overlap one another, or another row of a q_rope of the same strides,
+ *     are refused.
  * Rows, scales and query rows of no new token are left as they were.  A new_ptr or length that does
  * not fit, or a page outside the table or the pools, sets DCP_DEVERR_OUT_OF_RANGE and skips the
  * rows of that request or page.  Returns DCP_ERR_INVALID_ARG, DCP_ERR_CUDA.

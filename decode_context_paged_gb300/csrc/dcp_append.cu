@@ -14,7 +14,8 @@
 // turns for every p below 2^31, in integer instructions (the fp64 units are slow).
 //
 // Quantisation.  Block scales: the scale of g consecutive rows of a page is the smallest power of
-// two s with max|x| <= 448 s (non-finite values do not count; at least 2^-40).  A power of two makes
+// two s with max|x| <= 448 s (non-finite values do not count), held to [2^-40, 2^48]: the attention takes
+// larger scales as 2^48, so elements above 448 * 2^48 saturate here instead.  A power of two makes
 // x / s exact, costs no precision in E4M3's normal range, and lets a block's rows be coded again
 // with one more rounding only where they turn subnormal.  A call that goes on a block holding rows
 // of earlier tokens never shrinks its scale; where the scale grows the earlier rows are coded again.
@@ -45,7 +46,7 @@ namespace {
 
 constexpr int kRowsPerWarp = 4;
 constexpr int kQHeads = 8;              // heads one warp rotates: its loads are in flight together
-constexpr int kMinScaleExp = -40;
+constexpr int kMinScaleExp = -40, kMaxScaleExp = 48;
 
 // inv_freq / (2 pi) mod 1 as a 64-bit fraction.  x = m 2^(e - 1075) with an integer m < 2^53;
 // C = round(2^64 / (2 pi)); the fraction is m C 2^(e - 1075) as an integer modulo 2^64.
@@ -165,11 +166,11 @@ __device__ __forceinline__ uint32_t finite_amax(const uint4 &a, const uint4 &b, 
     return x;
 }
 
-// Smallest power of two s >= 2^-40 with amax <= 448 s (448 = 1.75 * 2^8).
+// Smallest power of two s >= 2^-40 with amax <= 448 s (448 = 1.75 * 2^8), at most 2^48.
 __device__ __forceinline__ float block_scale(uint32_t amax_bits) {
     const int e = (int)(amax_bits >> 23) - 127;
     const int k = e - 8 + ((amax_bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-    return __uint_as_float((uint32_t)(max(k, kMinScaleExp) + 127) << 23);
+    return __uint_as_float((uint32_t)(min(max(k, kMinScaleExp), kMaxScaleExp) + 127) << 23);
 }
 
 __device__ void rotate_queries(const AppendArgs &a, long long task, int lane) {

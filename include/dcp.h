@@ -418,10 +418,11 @@ int dcp_partial_decode_attn_static(int num_requests, int q_len, int num_heads, c
  *   dtype BF16: latent bits pass through, the rotated rope is rounded to nearest-even once.
  *   dtype E4M3, kv_scales NULL (scale_block 0): codes e4m3(x / kv_scale), saturating at 448.
  *   dtype E4M3, kv_scales: kv_scale must be 1.  A block's scale is the smallest power of two s
- *     >= 2^-40 with |x| <= 448 s for its finite new elements; codes e4m3(x / s): infinities saturate,
- *     NaN stays NaN, neither moves the scale.  A block that already holds rows of the request (its
- *     first new row is not the block's first) keeps the larger of its old scale and s; when it grows,
- *     the block's earlier rows are coded again as e4m3(code * old / new).
+ *     >= 2^-40 with |x| <= 448 s for its finite new elements, at most 2^48; codes e4m3(x / s): elements
+ *     above 448 s and infinities saturate, NaN stays NaN, neither infinities nor NaN move the scale.  A
+ *     block that already holds rows of the request (its first new row is not the block's first) keeps
+ *     the larger of its old scale and s; when it grows, the block's earlier rows are coded again as
+ *     e4m3(code * old / new).
  *   num_heads > 0: q_rope [num_new][num_heads][64] BF16 (given strides, even; 4-byte aligned), the
  *     new tokens' queries, are rotated alike into q_out, which may be q_rope itself with the same
  *     strides; rows of q_out that overlap one another, or another row of a q_rope of the same strides,

@@ -186,9 +186,9 @@ __device__ void rotate_queries(const AppendArgs &a, long long task, int lane) {
     const int b = warp_search(a.num_requests, tok, lane, [&](int i) { return (long long)__ldg(a.new_ptr + i); });
     if (b < 0) return;
     const long long n0 = __ldg(a.new_ptr + b), n1 = __ldg(a.new_ptr + b + 1);
-    if (tok >= n1 || n1 > a.num_new) return;  // a row no request has
+    if (n0 < 0 || tok >= n1 || n1 > a.num_new) return;  // a row no request has
     const long long start = (long long)__ldg(a.seq_lens + b) - (n1 - n0);
-    if (start < 0) return;  // reported by the request's unit
+    if (start < 0) return;  // (reported beside the units)
     const int fi = a.interleaved ? lane : 2 * (lane & 15);
     const unsigned long long f0 = turn_fraction(__ldg(a.inv_freq + fi));
     const unsigned long long f1 = a.interleaved ? 0 : turn_fraction(__ldg(a.inv_freq + fi + 1));
@@ -229,6 +229,7 @@ __global__ void __launch_bounds__(U * 8, 768 / (U * 8)) append_kernel(const __gr
     int lo = 0, hi = 0, d0 = 0;
     long long p0 = 0, p1 = 0;  // the request's page table
     uint32_t jj = 0;
+    auto fits = [&](long long n0, long long n1, int len) { return n0 >= 0 && n0 <= n1 && n1 <= a.num_new && n1 - n0 <= len; };
     if (warp == 0) {
         // x / (U ns): a unit's span of tokens
         auto spans = [&](uint32_t x) -> uint32_t { return TOK ? x / U / ns : x / U; };
@@ -259,9 +260,7 @@ __global__ void __launch_bounds__(U * 8, 768 / (U * 8)) append_kernel(const __gr
             p1 = __shfl_sync(0xffffffffu, page1, at);
             const int end = __shfl_sync(0xffffffffu, len, at);
             const uint32_t k = (uint32_t)(u - first_unit(n0, r0 + at));
-            if (n0 < 0 || n1 < n0 || n1 > a.num_new || n1 - n0 > end) {
-                if (n1 != n0 && k == 0 && lane == 0 && a.dev_error) atomicOr(a.dev_error, DCP_DEVERR_OUT_OF_RANGE);
-            } else if (n1 > n0) {
+            if (fits(n0, n1, end) && n1 > n0) {
                 const int start = end - (int)(n1 - n0);
                 jj = spans((uint32_t)start) + (TOK ? k / ns : k);
                 d0 = TOK ? (int)(k % ns) : 0;
@@ -285,6 +284,14 @@ __global__ void __launch_bounds__(U * 8, 768 / (U * 8)) append_kernel(const __gr
         }
     } else if (warp == 1) {
         fraction[lane] = turn_fraction(__ldg(a.inv_freq + lane));
+    } else if (warp == 2 && a.dev_error) {
+        // Requests that do not fit are reported here, 32 to a CTA (a request has two units at least): their
+        // offsets may lead to no unit at all.
+        const long long i = (long long)blockIdx.x * 32 + lane;
+        if (i < a.num_requests) {
+            const long long n0 = __ldg(a.new_ptr + i), n1 = __ldg(a.new_ptr + i + 1);
+            if (n0 != n1 && !fits(n0, n1, __ldg(a.seq_lens + i))) atomicOr(a.dev_error, DCP_DEVERR_OUT_OF_RANGE);
+        }
     }
     __syncthreads();
     lo = unit.lo;

@@ -175,15 +175,21 @@ __device__ __forceinline__ bool decode_unit(const Params &p, const T *q_ptr, con
     const int turn = (int)(c.x / (uint32_t)p.group);
     u.head = (int)c.y * p.group + (int)c.x - turn * p.group;
     if (u.head >= p.H) return false;
+    auto fits = [&](long long q0, long long q1, long long k0, long long k1) {
+        return q0 >= 0 && q0 <= q1 && q1 <= p.n_q && k0 >= 0 && k0 <= k1 && k1 <= p.n_k;
+    };
+    // Offsets that do not fit may lead to no slot at all: the first head's slots report them, 32 requests
+    // each (there are as many slots as requests, and more).
+    if (c.z == 0 && u.head == 0 && p.dev_error) {
+        const long long i = (long long)turn * 32 + lane;
+        if (i < p.B && !fits(q_ptr[i], q_ptr[i + 1], k_ptr[i], k_ptr[i + 1])) atomicOr(p.dev_error, DCP_DEVERR_OUT_OF_RANGE);
+    }
     const int slot = p.slots - 1 - turn;  // last rows first
     const int b = warp_search(p.B, slot, lane, [&](int i) { return (long long)(q_ptr[i] >> 8) + i; });
     if (b < 0) return false;
     const long long q0 = q_ptr[b], q1 = q_ptr[b + 1], k0 = k_ptr[b], k1 = k_ptr[b + 1];
     const long long r0 = (slot - ((q0 >> 8) + b)) * kUnitRows;
-    if (q0 < 0 || q1 < q0 || q1 > p.n_q || k0 < 0 || k1 < k0 || k1 > p.n_k) {
-        if (r0 == 0 && lane == 0 && p.dev_error) atomicOr(p.dev_error, DCP_DEVERR_OUT_OF_RANGE);
-        return false;
-    }
+    if (!fits(q0, q1, k0, k1)) return false;
     const int nq = (int)(q1 - q0), nk = (int)(k1 - k0);
     if (r0 >= nq) return false;
     u.valid = 1;
@@ -397,7 +403,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
             // Offsets of few requests are read once (each unit's decoding asks for them twice in a row).
             const bool cached = p.B <= kCached;
             for (int i = lane; cached && i <= p.B; i += 32) {
-                // (offsets that fit no tensor become -1, which decode_unit reports)
+                // (offsets that fit no tensor become -1, which fits no tensor either)
                 const long long a = p.q_ptr[i], b = p.k_ptr[i];
                 ctl->q_off[i] = a < 0 || a > p.n_q ? -1 : (int)a;
                 ctl->k_off[i] = b < 0 || b > p.n_k ? -1 : (int)b;

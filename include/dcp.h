@@ -429,7 +429,7 @@ int dcp_partial_decode_attn_static(int num_requests, int q_len, int num_heads, c
  *     are refused.
  * Rows, scales and query rows of no new token are left as they were.  A new_ptr or length that does
  * not fit, or a page outside the table or the pools, sets DCP_DEVERR_OUT_OF_RANGE and skips the
- * rows of that request or page.  Returns DCP_ERR_INVALID_ARG, DCP_ERR_CUDA.
+ * rows of that request or page (where new_ptr decreases, maybe rows of other requests too).  Returns DCP_ERR_INVALID_ARG, DCP_ERR_CUDA.
  */
 int dcp_append_kv(int num_requests, int64_t num_new, const void *latent, int64_t latent_stride, const void *rope,
                   int64_t rope_stride, const int64_t *new_ptr, const int32_t *seq_lens, const int64_t *req_page_ptr,
@@ -484,7 +484,8 @@ int dcp_decode_attn_merged_scaled(int num_requests, int q_len, int num_heads, co
  * Accuracy: scores and sums in fp32, weights rounded to BF16 (at most 2^-8 of each).
  * workspace (256-byte aligned): dcp_prefill_attn_workspace_size bytes for the same sizes; 0 for most,
  * more where few query rows face many keys and the keys are split over the SMs.
- * Offsets that do not fit set DCP_DEVERR_OUT_OF_RANGE; that request's rows are left undefined.
+ * Offsets that do not fit set DCP_DEVERR_OUT_OF_RANGE; that request's rows are left undefined (where
+ * offsets decrease, maybe rows of other requests too).
  * Returns DCP_ERR_INVALID_ARG (n_q, n_k <= 2^30, n_q * H < 2^31, H <= 65535), DCP_ERR_WORKSPACE, DCP_ERR_CUDA.
  */
 size_t dcp_prefill_attn_workspace_size(int num_requests, int64_t n_q, int64_t n_k, int num_heads);

@@ -92,34 +92,21 @@ constexpr float kLazyTauSc = 3.f;
 #ifndef DCP_ATTN_P_BUFS_BF16
 #define DCP_ATTN_P_BUFS_BF16 1
 #endif
-#ifndef DCP_ATTN_K_SLOTS_F8
-#define DCP_ATTN_K_SLOTS_F8 4
-#endif
 #ifndef DCP_ATTN_P_BUFS_F8
 #define DCP_ATTN_P_BUFS_F8 1
 #endif
-// V-stream ring: slots of DCP_ATTN_V_BLOCKS_* blocks, a block being one M-tile of the P*V
-// product for the tile's 128 tokens (BF16: two 64-dim TMA boxes, 32 KB; E4M3: one 128-dim box,
-// 16 KB).
+// BF16: V-stream ring, slots of DCP_ATTN_V_BLOCKS_BF16 blocks, a block being one M-tile of the P*V
+// product for the tile's 128 tokens (two 64-dim TMA boxes, 32 KB).
 #ifndef DCP_ATTN_V_SLOTS_BF16
 #define DCP_ATTN_V_SLOTS_BF16 2
 #endif
 #ifndef DCP_ATTN_V_BLOCKS_BF16
 #define DCP_ATTN_V_BLOCKS_BF16 1
 #endif
-#ifndef DCP_ATTN_V_SLOTS_F8
-#define DCP_ATTN_V_SLOTS_F8 2
-#endif
-#ifndef DCP_ATTN_V_BLOCKS_F8
-#define DCP_ATTN_V_BLOCKS_F8 2
-#endif
 // E4M3: one ring for both products.  A tile's four 128-dim blocks of K rows (16 KB each: 128
 // latent dims x 2 pages) serve the score MMAs as K and stay resident until the P*V MMAs have
 // used them as V, so V is never loaded a second time; the 64-dim rope block has a slot of its
 // own and is freed by the score MMAs.  DCP_ATTN_D_SLOTS_F8 blocks = 2 tiles of lookahead.
-#ifndef DCP_ATTN_UNIFIED_F8
-#define DCP_ATTN_UNIFIED_F8 1
-#endif
 #ifndef DCP_ATTN_D_SLOTS_F8
 #define DCP_ATTN_D_SLOTS_F8 8
 #endif
@@ -128,12 +115,12 @@ template <bool F8>
 struct Cfg {
     // BF16: four K slots and one P buffer (measured: trading a K slot for a second P buffer is
     // slower), a V ring of 2 x 32 KB.  E4M3: the unified ring (8 x 16 KB + the rope slot).
-    static constexpr bool kUnified = F8 && DCP_ATTN_UNIFIED_F8;
-    static constexpr int kKSlots = kUnified ? DCP_ATTN_D_SLOTS_F8 : F8 ? DCP_ATTN_K_SLOTS_F8 : DCP_ATTN_K_SLOTS_BF16;
+    static constexpr bool kUnified = F8;
+    static constexpr int kKSlots = kUnified ? DCP_ATTN_D_SLOTS_F8 : DCP_ATTN_K_SLOTS_BF16;
     static constexpr int kPBufs = F8 ? DCP_ATTN_P_BUFS_F8 : DCP_ATTN_P_BUFS_BF16;
-    static constexpr int kVSlots = kUnified ? 0 : F8 ? DCP_ATTN_V_SLOTS_F8 : DCP_ATTN_V_SLOTS_BF16;
-    static constexpr int kVBlk = F8 ? DCP_ATTN_V_BLOCKS_F8 : DCP_ATTN_V_BLOCKS_BF16;  // M-tiles per V slot
-    static constexpr uint32_t kVSlotBytes = kVBlk * 32768u / (F8 ? 2u : 1u);
+    static constexpr int kVSlots = kUnified ? 0 : DCP_ATTN_V_SLOTS_BF16;
+    static constexpr int kVBlk = DCP_ATTN_V_BLOCKS_BF16;  // M-tiles per V slot
+    static constexpr uint32_t kVSlotBytes = kVBlk * 32768u;
     static constexpr int kVUnits = 4 / kVBlk;       // V-stream units per tile
     static constexpr uint32_t kOffRope = kKSlots * kKSlotBytes;             // unified ring: the rope slot
     static constexpr uint32_t kOffV = kOffRope + (kUnified ? 8192u : 0u);
@@ -184,8 +171,8 @@ constexpr size_t smem_bytes() { return Cfg<F8>::kPad + Cfg<F8>::kOffCtl + sizeof
 static_assert(smem_bytes<false>() <= 232448 && smem_bytes<true>() <= 232448, "shared memory budget");
 static_assert(Cfg<false>::kVSlots <= kMaxVSlots && Cfg<true>::kVSlots <= kMaxVSlots, "V ring slots");
 static_assert(Cfg<false>::kKSlots <= kMaxKSlots && Cfg<true>::kKSlots <= kMaxKSlots, "K ring slots");
-static_assert(Cfg<true>::kVUnits > 0 && Cfg<false>::kVUnits > 0, "V units per tile");
-static_assert(4 % Cfg<false>::kVBlk == 0 && 4 % Cfg<true>::kVBlk == 0, "V slot blocks divide the 4 M-tiles");
+static_assert(Cfg<false>::kVUnits > 0, "V units per tile");
+static_assert(4 % Cfg<false>::kVBlk == 0, "V slot blocks divide the 4 M-tiles");
 
 struct AttnMaps {
     CUtensorMap q[2];                  // BF16: [0] 64x64 boxes.  FP8 (hi|lo rows): [0] 128x64 SW128, [1] 64x64 SW64
@@ -250,33 +237,6 @@ __device__ __forceinline__ float reduce_scatter16(const float (&v)[16], int lane
         }
     }
     return rs_op<kMax>(r[0], __shfl_xor_sync(0xffffffffu, r[0], 1));
-}
-
-template <bool kMax>
-__device__ __forceinline__ float reduce_scatter32(const float (&v)[32], int lane) {
-    float r[16];
-    {
-        const bool upper = (lane & 16) != 0;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float send = upper ? v[i] : v[i + 16];
-            const float keep = upper ? v[i + 16] : v[i];
-            r[i] = rs_op<kMax>(keep, __shfl_xor_sync(0xffffffffu, send, 16));
-        }
-    }
-#pragma unroll
-    for (int half = 8, off = 8; half >= 1; half >>= 1, off >>= 1) {
-        const bool upper = (lane & off) != 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (i < half) {
-                const float send = upper ? r[i] : r[i + half];
-                const float keep = upper ? r[i + half] : r[i];
-                r[i] = rs_op<kMax>(keep, __shfl_xor_sync(0xffffffffu, send, off));
-            }
-        }
-    }
-    return r[0];
 }
 
 // 2^x with the hardware approximation (relative error about 2^-22; 2^-inf = 0).
@@ -390,7 +350,7 @@ __device__ void q_split_row(int row, int R, const __nv_bfloat16 *__restrict__ q,
 template <bool F8, bool SC>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ KParams p) {
-    static_assert(!SC || Cfg<F8>::kUnified, "block scales are for 8-bit pools in the unified ring");
+    static_assert(!SC || F8, "block scales are for 8-bit pools");
     using C = Cfg<F8>;
     constexpr float kLazyTau = SC ? kLazyTauSc : C::kLazyTauV;
     constexpr float kPMul = SC ? 1.f : kPScale;  // (SC: in the exponent already)
@@ -616,33 +576,27 @@ attn_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ KPara
                         }
                         ++kpos;
                         uint8_t *dst = kring + slot * kKSlotBytes;
-                        if (F8 && kb == 4) {  // rope: 64 dims, 64-byte swizzle, 4 KB per page
-                            mbar_arrive_expect_tx(&ctl->kfull[slot], 8192);
-                            tma_load_2d_hint(dst, &km[1], &ctl->kfull[slot], 512, r0, pol);
-                            tma_load_2d_hint(dst + 4096, &km[1], &ctl->kfull[slot], 512, r1, pol);
-                        } else {
-                            const int x = F8 ? kb * 128 : kb * 64;
-                            // unified ring: a block with rows past the sequence serves P*V too
-                            const bool via = C::kUnified && fix;
-                            uint64_t *bar = via ? &ctl->vland : &ctl->kfull[slot];
-                            if (C::kUnified) {
-                                via_land = via ? (via_land | (1u << slot)) : (via_land & ~(1u << slot));
-                                land_pending = via;
+                        const int x = F8 ? kb * 128 : kb * 64;
+                        // unified ring: a block with rows past the sequence serves P*V too
+                        const bool via = C::kUnified && fix;
+                        uint64_t *bar = via ? &ctl->vland : &ctl->kfull[slot];
+                        if (C::kUnified) {
+                            via_land = via ? (via_land | (1u << slot)) : (via_land & ~(1u << slot));
+                            land_pending = via;
+                        }
+                        mbar_arrive_expect_tx(bar, kKSlotBytes);
+                        tma_load_2d_hint(dst, &km[0], bar, x, r0, pol);
+                        tma_load_2d_hint(dst + 8192, &km[0], bar, x, r1, pol);
+                        if (via) {
+                            if (!mbar_wait(&ctl->vland, land_cnt & 1, abort_flag, p.dev_error, lim)) {
+                                ok = false;
+                                break;
                             }
-                            mbar_arrive_expect_tx(bar, kKSlotBytes);
-                            tma_load_2d_hint(dst, &km[0], bar, x, r0, pol);
-                            tma_load_2d_hint(dst + 8192, &km[0], bar, x, r1, pol);
-                            if (via) {
-                                if (!mbar_wait(&ctl->vland, land_cnt & 1, abort_flag, p.dev_error, lim)) {
-                                    ok = false;
-                                    break;
-                                }
-                                ++land_cnt;
-                                land_pending = false;
-                                clear_tail(dst, nv0, nv1);
-                                fence_proxy_async_smem();
-                                mbar_arrive(&ctl->kfull[slot]);
-                            }
+                            ++land_cnt;
+                            land_pending = false;
+                            clear_tail(dst, nv0, nv1);
+                            fence_proxy_async_smem();
+                            mbar_arrive(&ctl->kfull[slot]);
                         }
                     }
                 }
@@ -765,13 +719,12 @@ attn_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ KPara
                         via_land = fix ? (via_land | (1u << slot)) : (via_land & ~(1u << slot));
                         land_pending = fix;
                         mbar_arrive_expect_tx(bar, C::kVSlotBytes);
-                        // the slot holds kBoxCols columns of 128-byte boxes (64 BF16 / 128 E4M3
-                        // dims), each of both pages: [box column][page][64 rows][128 B]
+                        // the slot holds kBoxCols columns of 128-byte boxes (64 dims), each of
+                        // both pages: [box column][page][64 rows][128 B]
                         constexpr int kBoxCols = (int)(C::kVSlotBytes / 16384);
-                        const int w = F8 ? 128 : 64;
 #pragma unroll
                         for (int h = 0; h < kBoxCols; ++h) {
-                            const int x = (kBoxCols * vu + h) * w;
+                            const int x = (kBoxCols * vu + h) * 64;
                             tma_load_2d_hint(dst + h * 16384, km, bar, x, r0, pol);
                             tma_load_2d_hint(dst + h * 16384 + 8192, km, bar, x, r1, pol);
                         }
@@ -827,13 +780,6 @@ attn_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ KPara
                 tc_fence_after();
                 // FP8: P's hi and lo terms, each 4 steps of 32 tokens; BF16: 8 steps of 16
                 const uint32_t p_lo = F8 ? desc_lo(pb, 512) : desc_lo(pb, 1024);
-                auto pv_f8 = [&](uint32_t d_tmem, uint32_t a0) {
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        mma_f8_ss_if(go, d_tmem, a0 + 256 * kk, hi128, p_lo + 128 * kk, hi64, C::kIdescPV, (i | kk) != 0);
-                        mma_f8_ss_if(go, d_tmem, a0 + 256 * kk, hi128, p_lo + 512 + 128 * kk, hi64, kIdescLo, 1);
-                    }
-                };
                 if constexpr (C::kUnified) {
                     // the tile's four latent blocks, still in the ring since its score MMAs
 #pragma unroll
@@ -845,7 +791,12 @@ attn_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ KPara
                         }
                         ++vpos;
                         tc_fence_after();
-                        pv_f8(tmem + 64 * m, desc_lo(kaddr + slot * kKSlotBytes, 16384));
+                        const uint32_t a_lo = desc_lo(kaddr + slot * kKSlotBytes, 16384), d_tmem = tmem + 64 * m;
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            mma_f8_ss_if(go, d_tmem, a_lo + 256 * kk, hi128, p_lo + 128 * kk, hi64, C::kIdescPV, (i | kk) != 0);
+                            mma_f8_ss_if(go, d_tmem, a_lo + 256 * kk, hi128, p_lo + 512 + 128 * kk, hi64, kIdescLo, 1);
+                        }
                         mma_commit_if(go, &ctl->kempty[slot]);
                     }
                 } else {
@@ -862,15 +813,11 @@ attn_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ KPara
 #pragma unroll
                         for (int mt = 0; mt < C::kVBlk; ++mt) {  // M-tiles (128 V dims each) of the slot
                             const uint32_t d_tmem = tmem + 64 * (C::kVBlk * vu + mt);
-                            if (F8) {
-                                pv_f8(d_tmem, desc_lo(a0 + mt * 16384, 16384));
-                            } else {
-                                const uint32_t a_lo = desc_lo(a0 + mt * 32768, 16384);
+                            const uint32_t a_lo = desc_lo(a0 + mt * 32768, 16384);
 #pragma unroll
-                                for (int kk = 0; kk < 8; ++kk)
-                                    mma_f16_ss_if(go, d_tmem, a_lo + 128 * kk, hi128, p_lo + 128 * kk, hi128, C::kIdescPV,
-                                                  (i | kk) != 0);
-                            }
+                            for (int kk = 0; kk < 8; ++kk)
+                                mma_f16_ss_if(go, d_tmem, a_lo + 128 * kk, hi128, p_lo + 128 * kk, hi128, C::kIdescPV,
+                                              (i | kk) != 0);
                         }
                         mma_commit_if(go, &ctl->vempty[slot]);
                     }

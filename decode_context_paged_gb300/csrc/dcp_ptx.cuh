@@ -194,18 +194,8 @@ __device__ __forceinline__ void tc_fence_after() {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
-// D[tmem] (+)= A[smem desc] * B[smem desc]^T, kind::f16 (BF16/F16 inputs, FP32 accumulate).
-__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                           uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
-// The forms below are for a warp in step: every lane runs them, the lane with issue != 0 (warp_elect) issues.
+// The MMAs and their commit are for a warp in step: every lane runs them, the lane with issue != 0 (warp_elect)
+// issues.  A and B in shared memory are given by the low and high words of their descriptors.
 __device__ __forceinline__ uint32_t warp_elect() {
     uint32_t e;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
@@ -291,31 +281,13 @@ __device__ __forceinline__ void mma_f16_ss_if(uint32_t issue, uint32_t d_tmem, u
         : "memory");
 }
 
+// Arrive (once) on `bar` when every tcgen05 op the issuing lane issued so far has completed.
 __device__ __forceinline__ void mma_commit_if(uint32_t issue, uint64_t *bar) {
     asm volatile(
         "{\n\t.reg .pred q;\n\t"
         "setp.ne.b32 q, %1, 0;\n\t"
         "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
         ::"r"(smem_u32(bar)), "r"(issue)
-        : "memory");
-}
-
-// D[tmem] (+)= A[smem desc] * B[smem desc]^T, kind::f8f6f4 (8-bit inputs, FP32 accumulate).
-__device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                          uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
-// Arrive (once) on `bar` when every tcgen05 op this thread issued so far has completed.
-__device__ __forceinline__ void mma_commit(uint64_t *bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-        ::"r"(smem_u32(bar))
         : "memory");
 }
 
@@ -410,28 +382,12 @@ __device__ __forceinline__ void tmem_wait_st() {
 constexpr uint32_t kSwizzle128 = 2;
 constexpr uint32_t kSwizzle64 = 4;
 
-__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes,
-                                              uint32_t layout) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-    d |= (uint64_t)((lbo_bytes >> 4) & 0x3FFFu) << 16;
-    d |= (uint64_t)((sbo_bytes >> 4) & 0x3FFFu) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)layout << 61;
-    return d;
-}
-
-// The words of such a descriptor: low (address, leading offset), high (stride, version, layout).
+// The words of a descriptor: low (address, leading offset), high (stride, version, layout).
 __host__ __device__ constexpr uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
     return ((saddr >> 4) & 0x3FFFu) | (((lbo_bytes >> 4) & 0x3FFFu) << 16);
 }
 __host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo_bytes, uint32_t layout) {
     return ((sbo_bytes >> 4) & 0x3FFFu) | (1u << 14) | (layout << 29);
-}
-
-__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo_bytes,
-                                                    uint32_t sbo_bytes) {
-    return smem_desc(saddr, lbo_bytes, sbo_bytes, kSwizzle128);
 }
 
 // Instruction descriptor, kind::f16: FP32 accumulate, BF16 A and B, given majorness

@@ -605,7 +605,6 @@ def partial_decode_attn(q: torch.Tensor, seq_lens: torch.Tensor, req_page_ptr: t
     num_pages = dst_vpages.numel()
     if workspace is None:
         workspace = _new((_workspace_bytes(B, T, H, N, num_pages),), torch.uint8, dev, stream)
-    kp = _ptr_array(kv_pools, "kv_pools")
     if kv_scales is not None:
         if layout not in ("page", "token"):
             raise ValueError("layout must be 'page' or 'token'")
@@ -620,6 +619,7 @@ def partial_decode_attn(q: torch.Tensor, seq_lens: torch.Tensor, req_page_ptr: t
             layout == "token", planned, _ptr(dev_error, "dev_error", torch.int32, d), _raw_stream(stream, d)),
                "dcp_partial_decode_attn_scaled")
         return o_part, lse_part
+    kp = _ptr_array(kv_pools, "kv_pools")
     fn = (_load().dcp_partial_decode_attn_run if planned else
           _load().dcp_partial_decode_attn_tokens if layout == "token" else _load().dcp_partial_decode_attn)
     _check(fn(B, T, H, _dptr(q, "q", torch.bfloat16),

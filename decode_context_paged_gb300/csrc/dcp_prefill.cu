@@ -168,6 +168,19 @@ struct Cta {  // a unit: grid (slots x heads of a group, groups, splits)
     uint32_t x, y, z;
 };
 
+__device__ __forceinline__ bool offsets_fit(const Params &p, long long q0, long long q1, long long k0, long long k1) {
+    return q0 >= 0 && q0 <= q1 && q1 <= p.n_q && k0 >= 0 && k0 <= k1 && k1 <= p.n_k;
+}
+
+// Offsets that do not fit may lead to no slot at all: the slots of head 0 report them, 32 requests each
+// (there are as many slots as requests, and more).  Called when a unit's loads are on their way.
+__device__ __noinline__ void report_offsets(const Params &p, Cta c, int lane) {
+    const uint32_t turn = c.x / (uint32_t)p.group;
+    const long long i = (long long)turn * 32 + lane;
+    if (c.x == turn * p.group && i < p.B && !offsets_fit(p, p.q_ptr[i], p.q_ptr[i + 1], p.k_ptr[i], p.k_ptr[i + 1]))
+        atomicOr(p.dev_error, DCP_DEVERR_OUT_OF_RANGE);
+}
+
 // A unit's rows and key tiles; false: the slot holds no rows.  (Warp-uniform.)
 template <typename T>
 __device__ __forceinline__ bool decode_unit(const Params &p, const T *q_ptr, const T *k_ptr, Cta c, int lane, Unit &u) {
@@ -175,21 +188,12 @@ __device__ __forceinline__ bool decode_unit(const Params &p, const T *q_ptr, con
     const int turn = (int)(c.x / (uint32_t)p.group);
     u.head = (int)c.y * p.group + (int)c.x - turn * p.group;
     if (u.head >= p.H) return false;
-    auto fits = [&](long long q0, long long q1, long long k0, long long k1) {
-        return q0 >= 0 && q0 <= q1 && q1 <= p.n_q && k0 >= 0 && k0 <= k1 && k1 <= p.n_k;
-    };
-    // Offsets that do not fit may lead to no slot at all: the first head's slots report them, 32 requests
-    // each (there are as many slots as requests, and more).
-    if (c.z == 0 && u.head == 0 && p.dev_error) {
-        const long long i = (long long)turn * 32 + lane;
-        if (i < p.B && !fits(q_ptr[i], q_ptr[i + 1], k_ptr[i], k_ptr[i + 1])) atomicOr(p.dev_error, DCP_DEVERR_OUT_OF_RANGE);
-    }
     const int slot = p.slots - 1 - turn;  // last rows first
     const int b = warp_search(p.B, slot, lane, [&](int i) { return (long long)(q_ptr[i] >> 8) + i; });
     if (b < 0) return false;
     const long long q0 = q_ptr[b], q1 = q_ptr[b + 1], k0 = k_ptr[b], k1 = k_ptr[b + 1];
     const long long r0 = (slot - ((q0 >> 8) + b)) * kUnitRows;
-    if (!fits(q0, q1, k0, k1)) return false;
+    if (!offsets_fit(p, q0, q1, k0, k1)) return false;
     const int nq = (int)(q1 - q0), nk = (int)(k1 - k0);
     if (r0 >= nq) return false;
     u.valid = 1;
@@ -524,6 +528,7 @@ prefill_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params
                     if (!ok) break;
                 }
                 if (!asked) ask();
+                if (p.dev_error && (idx.y | idx.z) == 0) report_offsets(p, idx, lane);
                 if (!wait(&ctl->answer_bar, (tries - 1) & 1)) {
                     ok = false;
                     break;

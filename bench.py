@@ -57,9 +57,9 @@ NCU_TRAFFIC = {
     ("reshard_kernel", "batch-32x8192-h64-q1-bf16-dcp8"): ("26b6b9b40d4d64dd", 552448000),
     ("reshard_kernel", "agent-48x100000-h64-q1-e4m3-dcp8"): ("26b6b9b40d4d64dd", 5236858368),
     ("reshard_kernel", "e2e-64x463936-h64-q1-e4m3-dcp8-L8-cp4"): ("26b6b9b40d4d64dd", 44745598653),
-    ("attn_kernel", "batch-32x8192-h64-q1-bf16-dcp8"): ("41661ead8cf55473", 324734976),
-    ("attn_kernel", "agent-48x100000-h64-q1-e4m3-dcp8"): ("41661ead8cf55473", 2786679808),
-    ("attn_kernel", "long-4x1048576-h64-q4-e4m3-dcp8"): ("41661ead8cf55473", 2517368832),
+    ("attn_kernel", "batch-32x8192-h64-q1-bf16-dcp8"): ("c79623fa338e8827", 324983040),
+    ("attn_kernel", "agent-48x100000-h64-q1-e4m3-dcp8"): ("c79623fa338e8827", 2786577664),
+    ("attn_kernel", "long-4x1048576-h64-q4-e4m3-dcp8"): ("c79623fa338e8827", 2517506048),
 }
 
 

@@ -28,8 +28,8 @@
 // floor(new_ptr[b] / W) + 2 b (W = the part's rows; times N and W = N rows for the token layout), which
 // bounds the pages its tokens can touch without a scan or a host copy.  Further CTAs of the same
 // launch rotate the queries.  Bound: launch latency for a decode step (64 tokens with 64 query
-// heads: 4.4 us), the latency of loads and barriers for prompts (69K tokens into E4M3 with blocks of
-// 16: 26.5 us = 4.5 TB/s, 67% of the copy rate).
+// heads: 4.0 us a call of a captured sequence), the latency of loads and barriers for prompts (69K tokens into E4M3 with blocks of
+// 16: 26.0 us = 4.55 TB/s, 68% of the copy rate).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>

@@ -10,9 +10,9 @@
 // and is read in place: no concatenated key is made.
 //
 // Design (GB300 / sm_103a).  Bound: the tensor cores (640 flops per key and query).  Measured: 8192
-// rows x 64 heads, causal, 753 us = 1.82 PFLOP/s, 95% of cuBLAS's BF16 rate (under a sustained power
-// cap 860 us); eight packed prompts of 1 to 2048 rows x 64 heads 145 us = 1.17 PFLOP/s; 256 rows over
-// 33,024 keys x 16 heads 75 us = 1.15 PFLOP/s and 3.7 TB/s.
+// rows x 64 heads, causal, 753 us = 1.82 PFLOP/s, 95% of cuBLAS's BF16 rate, at burst clocks, 820 to
+// 860 us under the power cap; eight packed prompts of 1 to 2048 rows x 64 heads 143 us = 1.18 PFLOP/s,
+// 154 to 159 us capped; 256 rows over 33,024 keys x 16 heads 73 us = 1.18 PFLOP/s and 3.8 TB/s.
 //  * A work unit is 256 query rows (two tiles of 128) of one request and head.  Per 128-key tile
 //    tcgen05 computes S_t = Q_t K^T (12 MMAs of 128 x 128 x 16) into TMEM, one softmax warpgroup per
 //    tile turns its S into P, and tcgen05 adds P_t V (8 MMAs, P read from TMEM) to O_t.  The two

@@ -498,7 +498,8 @@ int dcp_prefill_attn(int num_requests, int64_t n_q, int64_t n_k, int num_heads, 
 
 /*
  * The block scales of a reshard: what dcp_reshard_pages does with a block-scaled cache's pages,
- * for their scales.
+ * for their scales.  (Page layout only: dcp_token_reshard moves codes row by row and no scales; a
+ * token-interleaved cache gets block scales from dcp_append_kv.)
  *   src_scales (host array of n_cp device pointers): [layers of rank r][src_pool_pages][64 / scale_block]
  *   dst_scales (host array of n_dcp device pointers): [num_layers][dst_slots_per_rank][64 / scale_block]
  *   fp32, 4-byte aligned (16 is fastest where a page has four scales or more); layers are split over

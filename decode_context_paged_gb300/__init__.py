@@ -30,13 +30,24 @@ from __future__ import annotations
 
 import ctypes
 import os
+import re
+import sys
 from array import array
 
 import torch
 
+
+
+def _usable(views) -> bool:
+    """Whether the helper was built from this source's kind, for the running torch and Python: it reads
+    their objects with the layouts that it was compiled with."""
+    return (hasattr(views, "open") and getattr(views, "built_for_torch", "") == re.match(r"\d+(\.\d+)*", torch.__version__)[0]
+            and views.built_for_python == sys.hexversion >> 16)
+
+
 try:  # the questions and calls below in C++ (tensor_views.cpp), where it was built
     from . import _tensor_views as _views
-    if not hasattr(_views, "open"):  # built from an earlier source
+    if not _usable(_views):
         _views = None
 except ImportError:
     _views = None

@@ -48,9 +48,12 @@ def build_views(force: bool = False) -> None:
     """The binding's helper; without it (no compiler for it, no headers) the binding works all the same."""
     own_inc = os.path.join(os.path.dirname(PKG), "include")
     newest = max(os.path.getmtime(p) for p in (VIEWS_SRC, os.path.join(own_inc, "dcp.h"), os.path.abspath(__file__)))
-    if not force and os.path.exists(VIEWS) and os.path.getmtime(VIEWS) >= newest:
-        return
     import torch
+    built_for = f"{torch.__version__} {sys.version_info[:2]}\n"
+    stamp = os.path.join(BUILD_DIR, "tensor_views.txt")
+    old = open(stamp).read() if os.path.exists(stamp) else None
+    if not force and os.path.exists(VIEWS) and os.path.getmtime(VIEWS) >= newest and old == built_for:
+        return
     root = os.path.dirname(torch.__file__)
     lib = os.path.join(root, "lib")
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
@@ -70,6 +73,9 @@ def build_views(force: bool = False) -> None:
             os.remove(VIEWS)
         return
     os.replace(tmp, VIEWS)
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    with open(stamp, "w") as f:
+        f.write(built_for)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

@@ -16,6 +16,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/utils/object_ptr.h>
+#include <torch/version.h>
 
 #include <dlfcn.h>
 
@@ -194,4 +195,13 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_views", nullptr, -1, metho
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__tensor_views(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__tensor_views(void) {
+    PyObject *m = PyModule_Create(&module);
+    // what the layouts that this file was compiled with belong to: the binding uses no other
+    if (m && (PyModule_AddStringConstant(m, "built_for_torch", TORCH_VERSION) < 0 ||
+              PyModule_AddIntConstant(m, "built_for_python", PY_VERSION_HEX >> 16) < 0)) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}

@@ -3,6 +3,7 @@ CPU: a check that comes too late shows as another error.)"""
 import os
 import subprocess
 import sys
+import types
 
 import pytest
 import torch
@@ -52,6 +53,17 @@ def test_a_plan_needs_offsets_of_every_request():
     a = attention()
     with pytest.raises(ValueError, match="req_page_ptr holds 2"):
         dcp.attn_plan((2, 1, 4), torch.arange(2), a["dst_vpages"], a["kv_pools"], torch.zeros(1 << 20, dtype=torch.uint8))
+
+
+def test_a_helper_of_another_torch_or_python_is_not_used():
+    """It reads torch's objects by the layouts it was compiled with; the binding goes without it then."""
+    if dcp._views is None:
+        pytest.skip("the C++ helper was not built here")
+    have = dict(open=dcp._views.open, built_for_torch=dcp._views.built_for_torch, built_for_python=dcp._views.built_for_python)
+    assert dcp._usable(types.SimpleNamespace(**have))
+    for change in (dict(built_for_torch="1.0.0"), dict(built_for_python=0x030b)):
+        assert not dcp._usable(types.SimpleNamespace(**{**have, **change}))
+    assert not dcp._usable(types.SimpleNamespace(open=have["open"]))  # of an earlier source
 
 
 NO_STORAGE = """
